@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, kEight ? 4 : 1)
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   float gs = 1.f;
   if (a.h.grad_scale != nullptr) {
-    gs = __ldg(a.h.grad_scale);
+    gs = *a.h.grad_scale;
     if (!isfinite(gs)) return;
   }
   for (int i = threadIdx.x; i < a.n; i += kThreads) first[i] = a.chunk0[i];

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 2)
       float acc[NT] = {};
       float sw_v = 0.f;
       for (int j = k0; j < k1; ++j) {
-        if (((j - k0) & 31) == 0) sw_v = j + lane < k1 ? __ldg(sw + j + lane) : 0.f;
+        if (((j - k0) & 31) == 0) sw_v = j + lane < k1 ? sw[j + lane] : 0.f;
         const float w = __shfl_sync(0xffffffffu, sw_v, (j - k0) & 31);
         ok = warp_wait<kBrief>(smem_u32(&sxf[s]), sph, abort_flag, lim, p.status, W_PROM_SX, u) &&
              warp_wait<kBrief>(smem_u32(&accf[b]), bph, abort_flag, lim, p.status, W_PROM_ACCF, u);

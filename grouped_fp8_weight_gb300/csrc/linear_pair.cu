@@ -513,15 +513,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (from + 32 * i >= t.rows) {
               v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
             } else if (vec) {
-              const float4 q = __ldg(reinterpret_cast<const float4 *>(src));
+              const float4 q = *reinterpret_cast<const float4 *>(src);
               v[i][0] = q.x; v[i][1] = q.y; v[i][2] = q.z; v[i][3] = q.w;
             } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) v[i][k] = j + k < kb ? __ldg(src + k) : 0.f;
+              for (int k = 0; k < 4; ++k) v[i][k] = j + k < kb ? src[k] : 0.f;
             }
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = j + k < kb ? __ldg(sw + j + k) : 0.f;
+          for (int k = 0; k < 4; ++k) w[k] = j + k < kb ? sw[j + k] : 0.f;
         };
         load(0);
         for (int j = 0; j < kb; j += 4) {

@@ -49,7 +49,7 @@ __device__ void build_table(const LinearParams &p, const LinearTable &tab, int64
   bool bad = false;
   for (int e0 = 0; e0 < p.G; e0 += blockDim.x) {
     const int e = e0 + threadIdx.x;
-    const int m = e < p.G ? __ldg(p.ms + e) : 0;
+    const int m = e < p.G ? p.ms[e] : 0;
     bad |= m < 0;
     int64_t r = max(m, 0);
 #pragma unroll

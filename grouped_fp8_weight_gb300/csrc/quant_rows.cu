@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kThreads)
   if (static_cast<int>(blockIdx.x) >= blocks) {
     const int lane = threadIdx.x & 31, nw = (gridDim.x - blocks) * (kThreads / 32);
     for (int64_t r = (blockIdx.x - blocks) * (kThreads / 32) + (threadIdx.x >> 5); r < a.R; r += nw) {
-      if (__ldg(a.pairs + r) >= 0) continue;
+      if (a.pairs[r] >= 0) continue;
       for (int c = lane; c < pieces; c += 32) q[r * pieces + c] = make_uint4(0, 0, 0, 0);
       for (int b = lane; b < nb; b += 32) a.s[r * nb + b] = __fmul_rn(kFloor, kInv448);
     }
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (!live) continue;
     for (int j = 0; j < a.topk; ++j) {
-      const int r = __ldg(a.rows + t * a.topk + j);
+      const int r = a.rows[t * a.topk + j];
       if (r < 0) continue;
       if (r >= a.R) {
         atomicCAS(&a.status->code, DEV_OK, DEV_BAD_PAIR);

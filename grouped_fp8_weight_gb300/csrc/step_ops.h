@@ -52,7 +52,10 @@ cudaError_t launch_step(void (*kernel)(P...), unsigned grid, unsigned threads, s
 }
 #ifdef __CUDACC__
 // Lets the next kernel of the stream start as this one ends, and waits until
-// the one before has completed and its memory is visible.
+// the one before has completed and its memory is visible.  What that kernel may
+// have written is read with ordinary loads, which stay behind the wait: the
+// read-only path (__ldg) is for data that does not change while the kernel
+// runs, and this kernel may run while its inputs are being written.
 __device__ __forceinline__ void kernel_begin() {
   griddep_launch_dependents();
   griddep_wait();
