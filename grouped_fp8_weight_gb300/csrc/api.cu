@@ -19,6 +19,7 @@
 
 #include "dg_wgrad.h"
 #include "grouped_plan.h"
+#include "per_device.h"
 #include "step_ops.h"
 #include "wgrad_params.h"
 
@@ -59,7 +60,7 @@ struct DeviceState {
   cudaMemPool_t pool = nullptr;   // packed scale-factor scratch
 };
 
-constexpr int kMaxDevices = 64;
+using dg::kMaxDevices;
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
 

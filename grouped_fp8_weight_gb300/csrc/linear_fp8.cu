@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 
 #include "linear_table.cuh"
+#include "per_device.h"
 #include "step_ops.h"
 
 namespace dg {
@@ -289,8 +290,10 @@ template <int NT, bool kBrief>
 cudaError_t launch(const LinearParams &p, int sms, cudaStream_t stream) {
   using C = Cfg<NT>;
   const auto kernel = linear_kernel<NT, kBrief>;
-  static const cudaError_t set = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static OnceOnDevice once;
+  const cudaError_t set = once.run([&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  });
   if (set != cudaSuccess) return set;
   const int64_t tiles = linear_max_tiles(p.R, p.G, NT) * p.nb;
   // Measured (us with 1, 2, 4, 8 parts at most): 1 row of 4096 x 7168 20.3, 12.8,

@@ -51,6 +51,7 @@
 #include <cuda_bf16.h>
 
 #include "linear_table.cuh"
+#include "per_device.h"
 #include "step_ops.h"
 
 namespace dg {
@@ -553,13 +554,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool kBrief>
 cudaError_t launch(const LinearParams &p, int sms, cudaStream_t stream) {
   const auto kernel = linear_pair_kernel<kBrief>;
-  struct Setup {
-    cudaError_t err;
-    int max_pairs;
-  };
-  static const Setup setup = [&] {
-    Setup st{cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem), 0};
-    if (st.err != cudaSuccess) return st;
+  static PerDevice<int> resident;      // CTA pairs that fit the device
+  int max_pairs = 0;
+  const cudaError_t err = resident.get(&max_pairs, [&](int *n) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -571,13 +570,12 @@ cudaError_t launch(const LinearParams &p, int sms, cudaStream_t stream) {
     c.dynamicSmemBytes = kSmem;
     c.attrs = attr;
     c.numAttrs = 1;
-    st.err = cudaOccupancyMaxActiveClusters(&st.max_pairs, kernel, &c);
-    return st;
-  }();
-  if (setup.err != cudaSuccess) return setup.err;
+    return cudaOccupancyMaxActiveClusters(n, kernel, &c);
+  });
+  if (err != cudaSuccess) return err;
   const int64_t tiles = (p.R / kTok + std::min<int64_t>(p.R, p.G)) * ((p.N + 255) / 256);
   int64_t pairs = std::min<int64_t>(sms / 2, tiles);
-  if (setup.max_pairs > 0) pairs = std::min<int64_t>(pairs, setup.max_pairs);
+  if (max_pairs > 0) pairs = std::min<int64_t>(pairs, max_pairs);
   return launch_step(kernel, static_cast<unsigned>(2 * pairs), kThreads, kSmem, stream, 2, p);
 }
 

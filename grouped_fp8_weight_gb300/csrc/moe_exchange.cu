@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "per_device.h"
 #include "step_ops.h"
 
 namespace dg {
@@ -537,8 +538,11 @@ cudaError_t launch_moe_sort(const MoeSortArgs &a, int sms, cudaStream_t stream) 
     const unsigned threads =
         a.align > 1 ? kSortThreads : std::min(kSortThreads, std::max({32 * n_warps, (a.G + 31) / 32 * 32, 128}));
     const size_t smem = static_cast<size_t>(n_warps + 4) * a.G * sizeof(int);
-    static const cudaError_t set = cudaFuncSetAttribute(
-        sort_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 36 * 1024 * sizeof(int));
+    static OnceOnDevice once;
+    const cudaError_t set = once.run([] {
+      return cudaFuncSetAttribute(sort_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  36 * 1024 * sizeof(int));
+    });
     if (set != cudaSuccess) return set;
     return launch_step(sort_cluster_kernel, ctas, threads, smem, stream, ctas, a, n_warps, ctas);
   }

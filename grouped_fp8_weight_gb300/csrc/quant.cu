@@ -27,6 +27,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "per_device.h"
 #include "wgrad_params.h"
 
 namespace dg {
@@ -665,8 +666,8 @@ __global__ void __launch_bounds__(256, 3) gather_cast_kernel(const __grid_consta
 
 template <int kGran>
 cudaError_t launch_gather_tma(const CastArgs &a, cudaStream_t stream) {
-  // attributes set once per process (thread-safe static initialisation)
-  static const cudaError_t setup = [] {
+  static OnceOnDevice once;
+  const cudaError_t setup = once.run([] {
     cudaError_t e = cudaFuncSetAttribute(gather_cast_kernel<kGran>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kGtSmem);
     if (e == cudaSuccess)
@@ -674,7 +675,7 @@ cudaError_t launch_gather_tma(const CastArgs &a, cudaStream_t stream) {
                                cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
     return e;
-  }();
+  });
   if (setup != cudaSuccess) return setup;
   const dim3 grid(static_cast<unsigned>((a.T + kTileT - 1) / kTileT),
                   static_cast<unsigned>((a.C + kTileC - 1) / kTileC));
@@ -704,14 +705,15 @@ template <bool kGather>
 cudaError_t launch_requant_tm(const CastArgs &a, int gran_k, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((a.T + kTileT - 1) / kTileT),
                   static_cast<unsigned>((a.C + kRqTileC - 1) / kRqTileC));
-  static const cudaError_t setup = [] {
+  static OnceOnDevice once;
+  const cudaError_t setup = once.run([] {
     cudaError_t e = cudaFuncSetAttribute(requant_tm_kernel<128, kGather>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kRqSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(requant_tm_kernel<32, kGather>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, kRqSmem);
     return e;
-  }();
+  });
   if (setup != cudaSuccess) return setup;
   if (gran_k == 128)
     requant_tm_kernel<128, kGather><<<grid, 256, kRqSmem, stream>>>(a);

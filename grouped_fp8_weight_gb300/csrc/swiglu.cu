@@ -24,6 +24,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "per_device.h"
 #include "wgrad_params.h"
 
 namespace dg {
@@ -297,9 +298,11 @@ __global__ void __launch_bounds__(256, 2) swiglu_bwd_cast_kernel(const __grid_co
 
 template <int kGran, bool kWithA>
 cudaError_t launch_sg(const SwigluArgs &p, int ctas, cudaStream_t stream) {
-  // attribute set once per process (thread-safe static initialisation)
-  static const cudaError_t setup = cudaFuncSetAttribute(
-      swiglu_bwd_cast_kernel<kGran, kWithA>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSgSmem);
+  static OnceOnDevice once;
+  const cudaError_t setup = once.run([] {
+    return cudaFuncSetAttribute(swiglu_bwd_cast_kernel<kGran, kWithA>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSgSmem);
+  });
   if (setup != cudaSuccess) return setup;
   const int64_t tiles = static_cast<int64_t>(p.n_tt) * p.n_tc;
   const int grid = static_cast<int>(tiles < ctas ? tiles : ctas);

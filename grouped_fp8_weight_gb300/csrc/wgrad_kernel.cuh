@@ -69,6 +69,7 @@
 #define DG_ISSUE if (mma_el)
 #define DG_MMA_OK(x) (__all_sync(0xffffffffu, (x)))
 
+#include "per_device.h"
 #include "wgrad_params.h"
 
 namespace dg {
@@ -1257,23 +1258,20 @@ cudaError_t launch_wgrad_variant(const WgradParams &p, int pairs, cudaStream_t s
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // Shared-memory attribute and the number of co-resident pairs, once per
-  // process (thread-safe static initialisation).
-  struct Setup {
-    cudaError_t err;
-    int max_pairs;
-  };
-  static const Setup setup = [&] {
-    Setup st{cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  Cfg::SMEM_BYTES), 0};
-    if (st.err != cudaSuccess) return st;
+  // Shared-memory attribute and the number of co-resident pairs, once for each
+  // device.
+  static PerDevice<int> resident;
+  int max_pairs = 0;
+  const cudaError_t err = resident.get(&max_pairs, [&](int *n) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Cfg::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t c = cfg;
     c.gridDim = dim3(2 * (pairs > 0 ? pairs : 1), 1, 1);
-    st.err = cudaOccupancyMaxActiveClusters(&st.max_pairs, kern, &c);
-    return st;
-  }();
-  if (setup.err != cudaSuccess) return setup.err;
-  if (setup.max_pairs > 0) pairs = min(pairs, setup.max_pairs);
+    return cudaOccupancyMaxActiveClusters(n, kern, &c);
+  });
+  if (err != cudaSuccess) return err;
+  if (max_pairs > 0) pairs = min(pairs, max_pairs);
   cfg.gridDim = dim3(2 * pairs, 1, 1);
   if (kFP8 && p.pdl) cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, p);
