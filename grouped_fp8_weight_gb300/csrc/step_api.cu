@@ -169,15 +169,17 @@ dg_status dg_quant_rows_fp8(const void *x, int64_t T, int C, int topk, const int
                             const int *pair_rows, int64_t R, void *q, float *s_out,
                             dg_stream_t stream) {
   const char *fn = "dg_quant_rows_fp8";
-  if ((row_of_pair == nullptr) != (pair_rows == nullptr))
+  // (an empty map may be NULL: no tokens, or no rows)
+  const bool map = row_of_pair != nullptr || pair_rows != nullptr;
+  if (map && ((T > 0 && row_of_pair == nullptr) || (R > 0 && pair_rows == nullptr)))
     return failf(DG_ERR_INVALID_ARG, "%s: row_of_pair and pair_rows go together", fn);
   dg_status s = check_rows(fn, T, topk, R, C, 16);
   if (s != DG_OK) return s;
-  if (row_of_pair == nullptr && (R != T || topk != 1))
+  if (!map && R + T > 0 && (R != T || topk != 1))
     return failf(DG_ERR_INVALID_ARG, "%s: without a row map R must be T and topk 1", fn);
   if (R == 0) return done(fn, cudaSuccess);
   if (!aligned(q) || !aligned(s_out) || (T > 0 && !aligned(x)) ||
-      (pair_rows != nullptr && (!aligned(pair_rows) || !aligned(row_of_pair))))
+      (map && (!aligned(pair_rows) || (T > 0 && !aligned(row_of_pair)))))
     return bad_pointers(fn);
   dg::DeviceCtx dev;
   if ((s = dg::device_ctx(&dev)) != DG_OK) return s;

@@ -553,8 +553,9 @@ dg_status dg_moe_combine_backward(const void *dy, const void *ye, dg_dtype dtype
  *
  *   x   BF16 [T, C], finite; C a positive multiple of 16.
  *   row_of_pair, pair_rows  both NULL (then R = T, topk = 1 and row t is row
- *       t), or as for dg_moe_dispatch; rows that no pair owns get codes 0 and
- *       the smallest scale, 2^-100 * fl(1 / 448).
+ *       t), or as for dg_moe_dispatch (one that has no entries may be NULL);
+ *       rows that no pair owns get codes 0 and the smallest scale, 2^-100 *
+ *       fl(1 / 448).
  *   q   E4M3 [R, C];  s  FP32 [R, ceil(C / 128)].
  */
 dg_status dg_quant_rows_fp8(const void *x, int64_t T, int C, int topk, const int *row_of_pair,
