@@ -266,13 +266,19 @@ struct Four {
   // The step on the block whose lane this is (8 bits: the whole warp's);
   // `index` is the first element's.  Elements past the tensor's end hold zeros
   // and stay without effect on the block's scale.  sbyte: the new scale bytes,
-  // m's in the low half.  bm: b1 times m's old scale; vs: r's old scale.
+  // m's in the low half.  bm: b1 times m's old scale, or, where that is below the
+  // normal numbers and would lose bits, less that scale; vs: r's old scale.
   __device__ __forceinline__ void step(const AdamwHyper &h, float gs, uint32_t index, uint32_t key,
                                        float bm, float vs, uint32_t &sbyte) {
     float r[4];
     if constexpr (kEight) {
       decode4(mc, m);
       decode4(vc, v);
+      if (bm < 0.f) {                                // warp-uniform; blocks of zeros, all but always
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = __fmul_rn(m[k], -bm);
+        bm = h.b1;
+      }
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -373,7 +379,9 @@ __global__ void __launch_bounds__(kThreads, kEight ? 4 : 1)
     const bool has_block = lane * kBlock < len;
     if constexpr (kEight) {
       if (has_block) {
-        bm = __fmul_rn(a.h.b1, scale_value(e.sm[base / kBlock + lane]));   // exact: a power of two
+        const float s = scale_value(e.sm[base / kBlock + lane]);
+        bm = __fmul_rn(a.h.b1, s);          // exact where it is a normal number
+        if (bm < 0x1p-126f) bm = -s;
         vs = scale_value(e.sv[base / kBlock + lane]);
       }
     }
