@@ -22,8 +22,8 @@
 // the division of the update alone is the approximate one (2 ulp of an update
 // that is itself a small part of p).
 //
-// A non-finite moment is stored as NaN and takes no part in its block's
-// scale.  A non-finite grad_scale leaves every tensor untouched: the usual
+// A code has its moment's sign, zeros included.  A non-finite moment is stored
+// as NaN, code 0x7F, and takes no part in its block's scale.  A non-finite grad_scale leaves every tensor untouched: the usual
 // answer to a gradient norm that overflowed.
 //
 // Bound by memory: per element 24 + g bytes with FP32 states (g = 4 or 2 bytes
@@ -318,16 +318,19 @@ struct Four {
           cr[k] = encode(__fmul_rn(r[k], rs), rd, bits & 0xffffu);
         }
       }
-      if (odd) {
+      uint32_t sign = __byte_perm(__byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0073),
+                                  __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0073),
+                                  0x5410);
+      if (odd) {                                     // NaN is one code, without a sign
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          if (abs_bits(m[k]) >= kInfBits) cm[k] = 0x7f;
+          if (abs_bits(m[k]) >= kInfBits) {
+            cm[k] = 0x7f;
+            sign &= ~(0x80u << (8 * k));
+          }
           if (abs_bits(r[k]) >= kInfBits) cr[k] = 0x7f;
         }
       }
-      const uint32_t sign = __byte_perm(__byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0073),
-                                        __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0073),
-                                        0x5410);
       mc = (cm[0] + cm[1] * 0x100u + cm[2] * 0x10000u + cm[3] * 0x1000000u) | (sign & 0x80808080u);
       vc = cr[0] + cr[1] * 0x100u + cr[2] * 0x10000u + cr[3] * 0x1000000u;
       if ((vc - 0x01010101u) & ~vc & 0x80808080u) {  // a zero among the codes

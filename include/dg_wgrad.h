@@ -618,8 +618,10 @@ typedef struct dg_adamw_tensor {
  *   step        t, from 1.  betas in [0, 1).
  *   grad_scale  device FP32 scalar, or NULL for 1.  If it is not finite,
  *               nothing is written.
- * A non-finite gradient makes its element's moments NaN (8 bits: without
- * effect on its block's scale).
+ * A code of m has m's sign, zeros included.  A non-finite gradient makes its
+ * element's moments and parameter non-finite, one whose square overflows makes
+ * v infinite; with 8 bits a non-finite moment is code 0x7F (NaN), without
+ * effect on its block's scale.
  */
 dg_status dg_adamw_step(const dg_adamw_tensor *tensors, int n, dg_dtype grad_dtype,
                         int state_bits, int64_t step, double lr, double beta1, double beta2,

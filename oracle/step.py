@@ -128,7 +128,8 @@ def moment_decode(codes, scales):
 
 def moment_encode(x, bits16, keep):
     """(codes, scales) of float32 moments: rounded up with probability of the
-    part cut off, as bits16 / 2^16 decides; keep: above zero stays above zero."""
+    part cut off, as bits16 / 2^16 decides; keep: above zero stays above zero.
+    A code has its moment's sign, zeros included; what is not finite is 0x7F."""
     x = np.asarray(x, F)
     fin = np.isfinite(x)
     b = np.abs(_blocks(np.where(fin, x, F(0)))).astype(np.float64)
@@ -150,7 +151,7 @@ def moment_encode(x, bits16, keep):
     if keep:
         q = np.where((q == 0) & (b > 0), 2.0 ** -9, q)
     code = e4m3_encode(q).reshape(-1)[:x.size]
-    code = np.where((x < 0) & fin, code | 0x80, code)
+    code = np.where(np.signbit(x) & fin, code | 0x80, code)
     return np.where(fin, code, 0x7F).astype(np.uint8), (e + 127).astype(np.uint8)
 
 

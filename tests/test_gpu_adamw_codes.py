@@ -1,4 +1,5 @@
-"""AdamW's 8-bit moments byte for byte."""
+"""AdamW's 8-bit moments byte for byte: signs of zeros, moments that are not
+finite, and blocks at the bottom of FP32's range."""
 import numpy as np
 import pytest
 import torch
@@ -43,6 +44,42 @@ class State:
             got = code.cpu().numpy()
             assert np.array_equal(got, c), np.argwhere(got != c)[:4].tolist()
         return m1
+
+
+def test_codes_keep_the_sign_of_zero():
+    """Moments -0.0 and +0.0, and negative ones that round to zero."""
+    n = 300
+    m = np.where(np.arange(n) % 2, 0x80, 0x00)
+    g = np.where(np.arange(n) % 3, -0.0, 0.0)
+    g[0], g[128], g[256:] = 1.0, -1.0, np.where(np.arange(44) % 2, -1e-9, 1e-9)
+    g[260] = 1.0
+    s = State(g, m, np.zeros(n), np.full(3, 120), np.full(3, 120))
+    m1 = s.check(3, 11)
+    zero = (m1 == 0) & (np.arange(n) < 256)
+    got = s.m.cpu().numpy()
+    assert set(got[zero]) == {0x00, 0x80} and np.array_equal(got[zero] == 0x80, np.signbit(m1)[zero])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), -float("nan"), float("inf"), -float("inf")])
+def test_moments_that_are_not_finite_are_one_code(bad):
+    r = np.random.default_rng(1)
+    n = 400
+    g = r.standard_normal(n)
+    g[[0, 131, 399]] = bad
+    codes = r.integers(1, 127, (2, n))
+    codes[0] |= r.integers(0, 2, n) << 7
+    s = State(g, codes[0], codes[1], np.full(4, 120), np.full(4, 118))
+    s.check(7, 5)
+    assert set(s.m.cpu().numpy()[[0, 131, 399]]) == {0x7F}
+    assert set(s.v.cpu().numpy()[[0, 131, 399]]) == {0x7F}
+
+
+def test_a_negative_moment_that_was_not_finite_stays_one_code():
+    m = np.full(128, 0x3F)
+    m[5], m[6] = 0xFF, 0x7F
+    s = State(np.full(128, -0.5), m, np.full(128, 0x3F), np.full(1, 120), np.full(1, 120))
+    s.check(2, 3)
+    assert set(s.m.cpu().numpy()[[5, 6]]) == {0x7F}
 
 
 @pytest.mark.parametrize("byte,beta1,seed", [(0, 0.1, 0), (0, 0.1, 1), (1, 0.1, 1), (2, 0.1, 0),
