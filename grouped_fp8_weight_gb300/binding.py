@@ -582,6 +582,9 @@ def dg_adamw_step(plan, step: int, lr: float, beta1: float = 0.9, beta2: float =
     if grad_scale is not None:
         if grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or not grad_scale.is_cuda:
             raise ValueError("grad_scale: expected a float32 CUDA scalar")
+        if plan.device is not None and grad_scale.device != plan.device:
+            raise ValueError(f"grad_scale: expected a scalar on the plan's {plan.device}, got one on "
+                             f"{grad_scale.device}")
     n = len(plan.tensors[0])
     _check(lib().dg_adamw_step(
         plan.array, n, plan.grad_dtype, plan.state_bits, step, lr, beta1, beta2, eps,
