@@ -455,7 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idesc = __shfl_sync(0xffffffffu, idesc_f8(256, 0) | (n >> 3) << 17, 0);
         const bool turned = __shfl_sync(0xffffffffu, t.n, 0) != 0;
         const uint64_t a0 = turned ? w_desc0 : x_desc0, b0 = turned ? x_desc0 : w_desc0;
-        // a k-block, its sums into buffer kBuf
+        // A k-block, its sums into buffer kBuf.  Half of acce's arrivals are the
+        // partner's: behind them lie its tensor-memory reads and no memory that
+        // anyone writes, so the waits' CTA scope is enough (cluster scope for
+        // this wait 723 us against 714, for all of them 766, and with arrivals
+        // released at cluster scope too 1716).
         auto block = [&](auto buf_c) {
           constexpr int kBuf = decltype(buf_c)::value;
           if (!warp_wait<kBrief>(full0 + 8 * s, ph, abort_flag, lim, p.status, W_MMA_FULL, u) ||

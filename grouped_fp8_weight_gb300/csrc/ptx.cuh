@@ -146,10 +146,17 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
-// Bounded wait of a whole warp on a phase that this CTA's own threads, its TMA
-// loads or tensor-core commits complete (CTA-scope acquire, which unlike the
-// cluster-scope one leaves the L1 cache alone).  `bar` is a shared address.
-// Warp-uniform; same rules for the abort flag and the limit as mbar_wait.
+// Bounded wait of a whole warp on a phase behind which no other CTA's ordinary
+// memory writes lie: one that this CTA's own threads, TMA loads or tensor-core
+// commits complete, the pair's too, or that a partner's threads complete after
+// nothing but tensor-memory reads.  Its acquire is CTA-scope, which unlike the
+// cluster-scope one leaves the L1 cache alone.  That orders this CTA's threads;
+// what TMA and the tensor core wrote is complete when they signal the barrier;
+// and a partner's tcgen05.ld has completed (tcgen05.wait::ld) before its thread
+// arrives.  tc_fence_after() keeps later tcgen05 instructions behind the wait.
+// For a phase with another CTA's shared- or global-memory writes behind it there
+// is mbar_wait.  `bar` is a shared address.  Warp-uniform; same rules for the
+// abort flag and the limit as mbar_wait.
 __device__ __forceinline__ bool mbar_try_wait_cta(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
