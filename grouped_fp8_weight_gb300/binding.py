@@ -578,7 +578,8 @@ def dg_adamw_step(plan, step: int, lr: float, beta1: float = 0.9, beta2: float =
     """One AdamW step (the step-th, from 1) over the tensors of a plan, in
     place.  grad_scale: a float32 CUDA scalar that multiplies every gradient
     (if it is not finite nothing is written).  seed: with 8-bit states, another
-    one for each step."""
+    one for each step.  A graph that captures the call repeats its step number,
+    rates and seed at every replay."""
     if grad_scale is not None:
         if grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or not grad_scale.is_cuda:
             raise ValueError("grad_scale: expected a float32 CUDA scalar")

@@ -470,8 +470,11 @@ dg_status dg_k_grouped_fp8_wgrad_noalloc(const void *a, const uint8_t *sfa,
  * experts' forward FP8 product, and the optimizer that takes the weight
  * gradients.  Their formulas are the standard ones; the layouts and formats
  * are this library's.  Every call works on device counts and maps, waits for
- * nothing on the host and can be captured in a CUDA graph (dg_moe_sort up to
- * 2^15 pairs, where it needs no scratch).
+ * nothing on the host and can be captured in a CUDA graph: a replay is the same
+ * call again, on what its tensors hold then.  (A captured dg_moe_sort of more
+ * than 2^15 pairs takes its scratch from an allocation that the graph owns.)
+ * For dg_adamw_step that means the captured step number, rates and seed: an
+ * optimizer whose steps count on is called, or captured anew, at each step.
  *
  * dg_moe_sort -- token rows in expert order, from top-k routing.
  *
@@ -492,8 +495,9 @@ dg_status dg_k_grouped_fp8_wgrad_noalloc(const void *a, const uint8_t *sfa,
  *                padding rows and rows past the layout's end.
  *   src_rows     device int32 [cap] out or NULL: token t of each row, -1 likewise.
  *   cap          at least T * topk + G * (align - 1), below 2^31 - 256.
- * Scratch above 2^15 pairs: (chunks + 1) * G int32 of the device's pool,
- * chunks the 512-pair (at most 2048) pieces of the pairs.
+ * Scratch above 2^15 pairs: (chunks + 1) * G int32 of the device's pool (in a
+ * captured call, of the graph), chunks the 512-pair (at most 2048) pieces of the
+ * pairs.
  */
 dg_status dg_moe_sort(const int *topk_idx, int64_t T, int topk, int G, int align, int *counts,
                       int *row_of_pair, int *pair_rows, int *src_rows, int64_t cap,
