@@ -181,12 +181,14 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 uint64_t wait_limit_ns() {
-  // DG_WAIT_LIMIT_US (microseconds) takes precedence over DG_WAIT_LIMIT_MS.
+  // DG_WAIT_LIMIT_US (microseconds, a decimal number) takes precedence over
+  // DG_WAIT_LIMIT_MS.
   const char *us = std::getenv("DG_WAIT_LIMIT_US");
   if (us != nullptr && *us) {
     char *end = nullptr;
-    const long long v = std::strtoll(us, &end, 10);
-    if (end != us && v > 0) return static_cast<uint64_t>(v) * 1000ull;
+    const double v = std::strtod(us, &end);
+    if (end != us && v > 0)
+      return static_cast<uint64_t>(std::max(1.0, std::min(v * 1000.0, 1e18)));
   }
   const char *s = std::getenv("DG_WAIT_LIMIT_MS");
   long long ms = 4000;

@@ -43,10 +43,10 @@
  *    orientation and width, tiles, entries split along K, output mode) to
  *    stderr.
  *  - Device-side waits are bounded (default 4 s; environment variable
- *    DG_WAIT_LIMIT_US, else DG_WAIT_LIMIT_MS, read at each call).  A wait that
- *    runs out makes the kernel stop early and record DG_ERR_TIMEOUT in the
- *    device status word, which dg_sync_check() reports; the output is then
- *    unspecified.  Waits for copies already in flight, on the way out, keep a
+ *    DG_WAIT_LIMIT_US, a decimal number, else DG_WAIT_LIMIT_MS, read at each
+ *    call).  A wait that runs out makes the kernel stop early and record
+ *    DG_ERR_TIMEOUT in the device status word, which dg_sync_check() reports;
+ *    the output is then unspecified.  Waits for copies already in flight, on the way out, keep a
  *    limit of at least 2 s so that no copy outlives the kernel.
  *  - The MoE step calls launch their kernels as programmatic dependents: a
  *    kernel's CTAs may start while the kernel before it in the stream ends, and
