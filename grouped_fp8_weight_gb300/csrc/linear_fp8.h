@@ -20,7 +20,7 @@ struct LinearParams {
   const int *ms;        // [G] rows of each expert
   void *y;              // BF16 [R, N]
   int64_t R;
-  int G, N, K;
+  int G, N;
   int nb, kb;           // ceil(N / 128), ceil(K / 128)
   DevStatus *status;
   uint64_t wait_limit_ns;

@@ -528,8 +528,7 @@ size_t moe_sort_scratch_bytes(int64_t n, int G) {
   return static_cast<size_t>((chunks + 1) * G) * sizeof(int);
 }
 
-cudaError_t launch_moe_sort(const MoeSortArgs &a, int sms, cudaStream_t stream) {
-  (void)sms;
+cudaError_t launch_moe_sort(const MoeSortArgs &a, cudaStream_t stream) {
   if (a.n <= kSortOneCluster) {
     int ctas = 1;
     while (ctas < kSortCluster && (a.n > 32ll * kSortWarpPairs * ctas || a.cap > kSortFillRows * ctas)) ctas *= 2;

@@ -96,7 +96,7 @@ dg_status dg_moe_sort(const int *topk_idx, int64_t T, int topk, int G, int align
     const cudaError_t e = cudaMallocFromPoolAsync(&a.scratch, bytes, dev.pool, st);
     if (e != cudaSuccess) return failf(DG_ERR_CUDA, "%s: scratch: %s", fn, cudaGetErrorString(e));
   }
-  const cudaError_t e = dg::launch_moe_sort(a, dev.sms, st);
+  const cudaError_t e = dg::launch_moe_sort(a, st);
   if (bytes > 0) cudaFreeAsync(a.scratch, st);   // after the kernels in stream order
   return done(fn, e);
 }
@@ -219,7 +219,6 @@ dg_status dg_m_grouped_fp8_linear(const void *x, const float *sx, const void *w,
   p.R = R;
   p.G = G;
   p.N = N;
-  p.K = K;
   p.nb = nb;
   p.kb = (K + 127) / 128;
   p.status = dev.status;

@@ -76,7 +76,7 @@ struct MoeSortArgs {
   DevStatus *status;
 };
 size_t moe_sort_scratch_bytes(int64_t n, int G);
-cudaError_t launch_moe_sort(const MoeSortArgs &a, int sms, cudaStream_t stream);
+cudaError_t launch_moe_sort(const MoeSortArgs &a, cudaStream_t stream);
 
 // `rows` is row_of_pair [T, topk], `pairs` is pair_rows [R].
 struct MoeMoveArgs {
