@@ -11,11 +11,14 @@
 // powers of two and v would need twice as many as r.  Codes are rounded up
 // with probability equal to the part cut off: E4M3 steps are 6 to 12 % apart
 // while v moves by 0.1 % a step, so rounding to nearest would hold v where it
-// is; this rounding is right on average.  The probability is decided by 16
-// bits of a hash of the element's index in its tensor, the tensor's place in
-// the list and the caller's seed: the same call gives the same bits.  r above
-// zero never becomes zero, which would leave m' / eps as the next update.
-// The new moments enter the update before they are rounded.
+// is.  This rounding is right on average for each new code, and so for m, whose
+// recursion is linear.  v's next step squares what is held, so steady gradients
+// leave v 3 to 6 % high, and r with a spread (rms) of 12 to 17 %, whatever b2
+// (normal gradients, b2 = 0.999: 4.3 % and 14.8 % measured).  The probability is decided by 16 bits of a hash of the element's
+// index in its tensor, the tensor's place in the list and the caller's seed: the
+// same call gives the same bits.  r above zero never becomes zero, which would
+// leave m' / eps as the next update.  The new moments enter the update before
+// they are rounded.
 //
 // Every operation that a code depends on is a correctly rounded FP32
 // operation in the order written above, so codes can be reproduced exactly;

@@ -616,6 +616,9 @@ typedef struct dg_adamw_tensor {
  * with the probability of the part cut off, decided by 16 bits of a hash of
  * (seed, place of the tensor in the list, element): give each step its own
  * seed.  r above zero never becomes zero.  The same call gives the same bits.
+ * Each code is right on average, m over many steps too; v, the square of a
+ * rounded r, settles 3 to 6 % high and r spreads by 12 to 17 % (rms) under
+ * steady gradients, whatever b2.
  *
  *   tensors     HOST array of n entries, read during the call only.
  *   grad_dtype  of every g;  state_bits 8 or 32, of every tensor.
