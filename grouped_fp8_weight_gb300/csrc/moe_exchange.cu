@@ -370,9 +370,9 @@ __device__ __forceinline__ void zero_unused_rows(const MoeMoveArgs &a, int piece
   }
 }
 
-// Rows of a token loaded together (1 and 8: equal within 2 %, 8 slower by 4 % for
-// one pair a token).
-constexpr int kRowsAhead = 4;
+// Rows of a token loaded together (with 4, tokens to one expert 1.7 % slower; with
+// 1, equal within 1 %).
+constexpr int kRowsAhead = 2;
 
 __global__ void __launch_bounds__(kRowThreads)
     dispatch_kernel(const MoeMoveArgs a, int pieces, int blocks) {
@@ -404,20 +404,21 @@ __global__ void __launch_bounds__(kRowThreads)
 constexpr int kSlots = 8;   // pairs of a token whose pieces are in flight together
 
 // kPer: pairs in flight together, topk rounded up to a power of two or kSlots:
-// slots past topk cost instructions.  With kSlots whatever topk is, tokens of
-// 1928 BF16 values to 1 and 2 experts each (35770 of them) took 96 and 108 us
-// instead of 56 and 67, 20000 of 2048 FP32 values to 4 139 instead of 118.  The
-// CTAs a multiprocessor: with three for one and two pairs 65 and 76 us, with two
-// for four 136, with three for eight 477 against 353 (a training batch's exchange).
+// slots past topk cost instructions.  Tokens of 1928 BF16 values to 1 and 2
+// experts each (35770 of them) take 53 and 64 us, 20000 of 2048 FP32 values to 4
+// 117; with kSlots whatever topk is an earlier form took 96, 108 and 139 instead
+// of 56, 67 and 118.  CTAs a multiprocessor, same form: with three for one and two
+// pairs 65 and 76 us, with two for four 136, with three for eight 477 against 353
+// (a training batch's exchange).  No form spills registers: the piece's place is
+// stepped along instead of divided out (with a division 12 to 64 bytes spilled).
 template <bool kBf16, int kPer>
 __global__ void __launch_bounds__(kRowThreads, kPer == 8 ? 2 : kPer == 4 ? 3 : 4)
-    combine_kernel(const MoeMoveArgs a, int pieces) {
+    combine_kernel(const MoeMoveArgs a, int pieces, int dt, int dc) {
   kernel_begin();
   using P = Piece<kBf16>;
   const uint4 *ye = static_cast<const uint4 *>(a.x);
   // this thread's pieces are a grid apart: dt tokens and dc pieces
-  const uint32_t first = blockIdx.x * kRowThreads + threadIdx.x, grid = gridDim.x * kRowThreads;
-  const int dt = grid / pieces, dc = grid % pieces;
+  const uint32_t first = blockIdx.x * kRowThreads + threadIdx.x;
   int c = first % pieces;
   for (int64_t t = first / pieces; t < a.T; t += dt) {
     float acc[P::N] = {};
@@ -581,13 +582,15 @@ cudaError_t launch_moe_dispatch(const MoeMoveArgs &a, int sms, cudaStream_t stre
 cudaError_t launch_moe_combine(const MoeMoveArgs &a, int sms, cudaStream_t stream) {
   const int pieces = a.C / (a.bf16 ? 8 : 4);
   const int blocks = blocks_for((a.T * pieces + kRowThreads - 1) / kRowThreads, sms);
-  void (*const kernels[4][2])(const MoeMoveArgs, int) = {
+  const int grid = blocks * kRowThreads;   // threads: below 2^31
+  void (*const kernels[4][2])(const MoeMoveArgs, int, int, int) = {
       {combine_kernel<false, 1>, combine_kernel<true, 1>},
       {combine_kernel<false, 2>, combine_kernel<true, 2>},
       {combine_kernel<false, 4>, combine_kernel<true, 4>},
       {combine_kernel<false, kSlots>, combine_kernel<true, kSlots>}};
   const int k = a.topk > 4 ? 3 : a.topk > 2 ? 2 : a.topk > 1 ? 1 : 0;
-  return launch_step(kernels[k][a.bf16 ? 1 : 0], blocks, kRowThreads, 0, stream, 1, a, pieces);
+  return launch_step(kernels[k][a.bf16 ? 1 : 0], blocks, kRowThreads, 0, stream, 1, a, pieces,
+                     grid / pieces, grid % pieces);
 }
 
 cudaError_t launch_moe_combine_backward(const MoeMoveArgs &a, int sms, cudaStream_t stream) {
