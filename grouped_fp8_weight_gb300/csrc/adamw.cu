@@ -14,11 +14,11 @@
 // is.  This rounding is right on average for each new code, and so for m, whose
 // recursion is linear.  v's next step squares what is held, so steady gradients
 // leave v 3 to 6 % high, and r with a spread (rms) of 12 to 17 %, whatever b2
-// (normal gradients, b2 = 0.999: 4.3 % and 14.8 % measured).  The probability is decided by 16 bits of a hash of the element's
-// index in its tensor, the tensor's place in the list and the caller's seed: the
-// same call gives the same bits.  r above zero never becomes zero, which would
-// leave m' / eps as the next update.  The new moments enter the update before
-// they are rounded.
+// (normal gradients, b2 = 0.999: 4.3 % and 14.8 % measured).  The probability is
+// decided by 16 bits of a hash of the element's index in its tensor, the tensor's
+// place in the list and the caller's seed: the same call gives the same bits.  r
+// above zero never becomes zero, which would leave m' / eps as the next update.
+// The new moments enter the update before they are rounded.
 //
 // Every operation that a code depends on is a correctly rounded FP32
 // operation in the order written above, so codes can be reproduced exactly;
@@ -26,13 +26,14 @@
 // that is itself a small part of p).
 //
 // A code has its moment's sign, zeros included.  A non-finite moment is stored
-// as NaN, code 0x7F, and takes no part in its block's scale.  A non-finite grad_scale leaves every tensor untouched: the usual
-// answer to a gradient norm that overflowed.
+// as NaN, code 0x7F, and takes no part in its block's scale.  A non-finite
+// grad_scale leaves every tensor untouched: the usual answer to a gradient norm
+// that overflowed.
 //
 // Bound by memory: per element 24 + g bytes with FP32 states (g = 4 or 2 bytes
 // of gradient), 12 + 1/32 + g with 8-bit ones, and 2 for a BF16 copy.  201 M
 // elements: 895 us with FP32 states and gradients and a copy (101 % of the copy
-// rate); 516 us with 8-bit states, BF16 gradients and a copy (93 %), where 69
+// rate); 517 us with 8-bit states, BF16 gradients and a copy (93 %), where 71
 // instructions per element keep the schedulers two thirds busy as well.
 //
 // The list travels in the kernel's parameters (up to 32 KB of them), so a

@@ -35,7 +35,8 @@ bool deterministic_requested();
 
 // DG_PDL=0 in the environment (read at each call) launches an FP8 GEMM only
 // after its scale-pack pass has completed, instead of as a programmatic
-// dependent that starts beside it.
+// dependent that starts beside it, and the MoE step's kernels after the one
+// before (step_ops.h).
 bool pdl_requested();
 
 struct GroupedArgs {

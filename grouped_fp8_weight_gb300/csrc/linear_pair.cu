@@ -17,10 +17,11 @@
 // rest tile a thread holds pairs of tokens of two rows (the 16-lane read), so
 // that it reads each scale pair once for four sums.
 //
-// Measured: 32768 rows over 32 skewed experts, 4096 x 7168, in 772 us (calls in
-// a row; 820 alone), 2490 TFLOP/s or 71 % of the dense FP8 rate that cuBLASLt
-// reaches here, at 1.6 to 1.8 GHz under the power cap (1365 of 1400 W).  A k-block of a full tile
-// takes 804 cycles, 512 of them MMAs; loads and scales are always there.  What
+// Measured: 32768 rows over 32 skewed experts, 4096 x 7168, in 722 us (50 calls
+// in a row; 2665 TFLOP/s, 76 % of the dense FP8 rate that cuBLASLt reaches here)
+// before the power cap, 809 us (2378 TFLOP/s) in a row of 6000 at a median of 1627
+// MHz under it (1366 of 1400 W); 714 to 830 us by box and length of the row.  A
+// k-block of a full tile takes 804 cycles, 512 of them MMAs; loads and scales are always there.  What
 // bounds it is the promoting warps' way round a buffer: 147 cycles until they
 // have seen its sums (57 % of the time these are there before them), 367 until
 // they have read them, 84 for the last sums, 40 for the output spread over 56

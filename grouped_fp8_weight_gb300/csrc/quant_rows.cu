@@ -11,8 +11,11 @@
 // gradually, and a padding row is codes 0 with the floor's scale.
 //
 // Bound by memory: 2 bytes read per element, and 1 + 1/32 written for every
-// row the token goes to.  Sixteen lanes hold a block, eight elements (one
-// 16-byte load) each, and reduce its maximum with four shuffles.
+// row the token goes to (16384 tokens of 7168 to 4 of 64 experts 121 us, 97 % of
+// the copy rate).  Eight lanes hold a block, sixteen elements (two 16-byte loads)
+// each, and reduce its maximum with three shuffles.  The row map is read entry
+// by entry: four entries ahead took 39 registers, and 10.0 us against 9.2 for 9000
+// tokens of 2048 to one expert.
 #include <algorithm>
 #include <cstdint>
 

@@ -576,13 +576,15 @@ dg_status dg_quant_rows_fp8(const void *x, int64_t T, int C, int topk, const int
  * expert e: [off_e, off_e + ms_dev[e]), off_e the sum of the counts before.
  * Any counts, zero included; rows past their sum are not written.  Block sums
  * are formed in the tensor core, scaled and added in FP32, and rounded once.
+ * The two scales of a block are multiplied first, in FP32: a product below
+ * 2^-126 loses bits, and one that overflows makes the row infinite or NaN.
  *
  *   x    E4M3 [R, K];  sx FP32 [R, ceil(K / 128)].
  *   w    E4M3 [G, N, K] (a linear layer's weight);
  *   sw   FP32 [G, ceil(N / 128), ceil(K / 128)].
  *   y    BF16 [R, N].
  *   K, N positive multiples of 16;  0 <= G <= DG_MAX_GROUPS;  R and G * N below
- *        2^31 - 256.
+ *        2^31 - 256, and (R / 16 + min(R, G)) * ceil(N / 128) below 2^28.
  *   ms_dev  device int32 [G].  A negative count (taken as zero) and counts that
  *        sum past R (the rows past R are left out) are recorded
  *        (dg_sync_check: DG_ERR_INVALID_ARG).
